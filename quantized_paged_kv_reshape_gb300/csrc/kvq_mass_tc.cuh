@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(544, 1) mass_tc_kernel(const MassArgs a, const
                         (a.window <= 0 || t0 > last - a.window);
       const uint8_t* okb = ok_s + (tile - tile0) % 3 * 128;
       uint32_t s[NC];
+      __syncwarp();   // (lanes fetched and stored different rows; the load is the whole warp's)
 #pragma unroll
       for (int c = 0; c < NC; c += 16) t5::ld16(src + c, *reinterpret_cast<uint32_t(*)[16]>(s + c));
       t5::wait_ld();

@@ -581,6 +581,7 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
       v_nonfinite = false;
     }
     if (!t5::wait(bar_s, par)) ok_all = false;
+    __syncwarp();   // each lane waited by itself; tensor-memory accesses are the whole warp's
     t5::fence_after();
 
     // ---- this part of the score row, masked only where the step cuts a range
@@ -699,6 +700,7 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
               v[j] = __float_as_uint(fmaf(p, y, __uint_as_float(v[j])));
             }
           }
+          __syncwarp();   // lanes left out other positions; the store is the whole warp's
           t5::st16(o_tm + t_lane + c0, v);
         }
         t5::wait_st();
@@ -767,6 +769,7 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) os[row * (HD + 4) + c0 + j] = have_o ? __uint_as_float(v[j]) * inv : 0.f;
       }
+      __syncwarp();   // the next load is the whole warp's
     }
   }
   if constexpr (SH) {

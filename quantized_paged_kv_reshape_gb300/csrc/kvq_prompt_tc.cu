@@ -538,6 +538,7 @@ prompt_tc_kernel(const PromptArgs a, const __grid_constant__ PromptMaps maps, in
         ++cuts;
       }
       if ((tid & 255) == 0) skip[buf] = by_hand;
+      __syncwarp();   // the loads below are the whole warp's
       // this half's scores, masked where the tile is cut
       const uint32_t m0 = (uint32_t)(lo - kv0 - 64 * half), span = (uint32_t)(i - lo);
       auto fetch = [&](uint32_t (&s)[64]) {

@@ -192,3 +192,29 @@ def test_shared_streams_and_graphs():
         d["q"].copy_(q)
         g.replay()
         assert torch.equal(out, w)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("hd,nq,nkv", [(64, 6, 2), (128, 8, 1), (256, 4, 2)])
+def test_shared_window_edge_with_nonfinite_values_of_many_members(fmt, hd, nq, nkv):
+    """Members of a tile whose windows start on either side of a position with
+    a NaN value: their rows differ in what they add, lane by lane."""
+    own = [1 + 3 * i for i in range(11)]
+    c = shared_case(fmt, [130], [11], own, nq, nkv, hd, seed=hd)
+    d = dev(c)
+    window = 100                          # starts 130 + own - 100: 31, 34, ..., 61
+    want = run(c, d, sliding_window=window)
+    pos, bs = 45, 16
+    row = d["vp"][int(c["ptab"][0, pos // bs])]
+    size = nkv * hd * (2 if fmt == "bf16" else 1)
+    bad = torch.tensor([0xFF, 0x7F], dtype=torch.uint8, device=DEV) if fmt == "bf16" else \
+        torch.tensor([0x7F], dtype=torch.uint8, device=DEV)
+    row[pos % bs * size:(pos % bs + 1) * size] = bad.repeat(size // bad.numel())
+    got = run(c, d, sliding_window=window)
+    sees = torch.tensor([30 + n <= pos for n in own], device=DEV)
+    assert torch.isnan(got[sees]).all()
+    # the step with the value is added in another order, and from weights in two
+    # 16-bit parts (2^-16 of a weight at most) as the products': sums of n terms
+    # each, (n + 2) 2^-24 max|v|
+    n = 130 + max(own)
+    assert (got[~sees] - want[~sees]).abs().max() <= 2 * (n + 2) * 2.0 ** -24 * np.abs(c["v"]).max()
