@@ -448,8 +448,9 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
     const int t = tid / PARTS, part = tid % PARTS;
     const bool ok = blk >= 0 && (a.num_blocks <= 0 || blk < a.num_blocks);
     const int64_t rr = (int64_t)((st * TOK + t) & (a.bs - 1)) * a.nkv + kvh;
-    if constexpr (SH) {
-      if (!ok && st * TOK + t < len && part == 0 && a.err) atomicOr(a.err, 2);   // KVQ_DEVERR_BLOCK
+    if constexpr (SH) {   // (a first step may begin before the lowest window start, where pages may be gone)
+      const int pos = st * TOK + t;
+      if (!ok && pos >= lo_first && pos < len && part == 0 && a.err) atomicOr(a.err, 2);   // KVQ_DEVERR_BLOCK
     }
     if (!ok) blk = 0;
     const uint8_t* kb = a.k_cache + blk * a.k_bstride;

@@ -218,3 +218,21 @@ def test_shared_window_edge_with_nonfinite_values_of_many_members(fmt, hd, nq, n
     # each, (n + 2) 2^-24 max|v|
     n = 130 + max(own)
     assert (got[~sees] - want[~sees]).abs().max() <= 2 * (n + 2) * 2.0 ** -24 * np.abs(c["v"]).max()
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("bs", [8, 16])
+def test_shared_pages_freed_before_the_window(hd, bs):
+    """Pages that lie wholly before every member's window may be gone from the
+    table: no flag, no difference.  One inside it is flagged."""
+    c = shared_case("bf16k_turbo4v", [100], [2], [20, 28], 8, 2, hd, bs=bs, seed=19)
+    d = dev(c)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    want = run(c, d, sliding_window=60, error_flag=err)   # from positions 60 and 68 on
+    d["ptab"][0, :60 // bs] = -1
+    got = run(c, d, sliding_window=60, error_flag=err)
+    assert err.item() == 0
+    assert torch.equal(got, want)
+    d["ptab"][0, 60 // bs] = -1
+    run(c, d, sliding_window=60, error_flag=err)
+    assert err.item() == _abi.KVQ_DEVERR_BLOCK
