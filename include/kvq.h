@@ -405,7 +405,10 @@ size_t kvq_shared_decode_workspace_bytes(int32_t num_seqs, int32_t num_groups,
  *   prefix_tables device int32 [num_groups, max_prefix_blocks]
  *   prefix_lens  device int32 [num_groups], >= 0
  *   cu_groups    device int32 [num_groups + 1], non-decreasing; sequences in no
- *                group have no prefix; num_groups >= 1
+ *                group have no prefix; num_groups >= 1.  Entries outside
+ *                [0, num_seqs] are cut and flagged (KVQ_DEVERR_RANGE); where
+ *                one is below the one before, no sequence has a prefix, and
+ *                that is flagged
  *   workspace    device, 16-byte aligned, >= kvq_shared_decode_workspace_bytes;
  *                calls that may run at the same time need separate ones (a
  *                captured graph's replays among them)

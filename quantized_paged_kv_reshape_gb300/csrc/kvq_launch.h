@@ -75,6 +75,7 @@ struct SharedArgs {
   float2* ml;                // [num_seqs][nq][splits] running maximum (base 2) and sum
   int32_t* counters;         // the decode's merge counters, zeroed for it
   int64_t num_counters;
+  int32_t* unordered;        // set to 1 where cu_q (cu_groups) decreases somewhere, else 0
 };
 
 struct PrefillArgs {  // arguments of the chunked prefill (prefill_tc5_kernel)

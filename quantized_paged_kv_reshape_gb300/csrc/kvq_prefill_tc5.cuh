@@ -256,6 +256,21 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
     const int64_t cta = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     for (int64_t i = cta * NT + tid; i < a.sh.num_counters; i += (int64_t)gridDim.x * gridDim.y * NT)
       a.sh.counters[i] = 0;
+    // Decreasing offsets have no groups (overlapping ones could need more
+    // ranges than there are CTAs): the join then takes the own positions alone.
+    bool dec = false, cut = false;
+    for (int g = lane; g < a.sh.num_groups; g += 32) {
+      const int m0 = a.cu_q[g], m1 = a.cu_q[g + 1];
+      dec |= m1 < m0;
+      cut |= m0 < 0 || m1 > a.num_seqs;
+    }
+    dec = __any_sync(0xffffffffu, dec);
+    cut = __any_sync(0xffffffffu, cut);
+    if (cta == 0 && tid == 0) {
+      *a.sh.unordered = dec;
+      if ((dec || cut) && a.err) atomicOr(a.err, 8);   // KVQ_DEVERR_RANGE
+    }
+    if (dec) return;
     const int64_t room = (int64_t)a.max_blocks * a.bs;
     auto group = [&](int g, int& tiles, int& steps) {   // tiles of its members, steps of its prefix
       const int m0 = max(a.cu_q[g], 0), m1 = min(a.cu_q[g + 1], a.num_seqs);

@@ -28,6 +28,7 @@ struct JoinArgs {
   const float* lse;     // [num_seqs][nq]
   const int32_t* cu_groups;
   const int32_t* prefix_lens;
+  const int32_t* unordered;
   int32_t num_groups, num_seqs, nq, splits;
   void* out;
   int out_bf16;
@@ -48,7 +49,7 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const JoinArgs a) {
     const int mid = (lo + hi) / 2;
     if (a.cu_groups[mid] <= seq) lo = mid; else hi = mid;
   }
-  const bool grouped = a.cu_groups[lo] <= seq && seq < a.cu_groups[lo + 1] && a.prefix_lens[lo] > 0;
+  const bool grouped = *a.unordered == 0 && a.cu_groups[lo] <= seq && seq < a.cu_groups[lo + 1] && a.prefix_lens[lo] > 0;
   const int n = grouped ? a.splits : 0;   // at most 64
   const float lse = a.lse[row];
   // lane i has parts i and i + 32; a part without positions is (-inf, 0)
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const JoinArgs a) {
 
 struct SharedPlan {
   int slots, splits;
-  size_t decode, own, lse, part, ml, total;   // byte offsets and the whole size
+  size_t decode, own, lse, part, ml, unordered, total;   // byte offsets and the whole size
 };
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -122,7 +123,8 @@ SharedPlan plan_shared(int32_t num_seqs, int32_t num_groups, int nq, int nkv, in
   p.lse = p.own + align256(rows_all * hd * 4);
   p.part = p.lse + align256(rows_all * 4);
   p.ml = p.part + align256(rows_all * p.splits * hd * 4);
-  p.total = p.ml + align256(rows_all * p.splits * 8);
+  p.unordered = p.ml + align256(rows_all * p.splits * 8);
+  p.total = p.unordered + 256;
   return p;
 }
 
@@ -225,6 +227,7 @@ kvq_status kvq_paged_decode_shared(const void* q, kvq_dtype q_dtype, int64_t q_s
   const size_t ctr = ((size_t)num_seqs * nkv * sizeof(int32_t) + 15) / 16 * 16;
   a.sh.counters = (int32_t*)(ws + dec - ctr);
   a.sh.num_counters = (int64_t)num_seqs * nkv;
+  a.sh.unordered = (int32_t*)(ws + p.unordered);
   const Codebooks& cb = codebooks();
   cudaError_t e;
   switch (ks) {
@@ -244,7 +247,7 @@ kvq_status kvq_paged_decode_shared(const void* q, kvq_dtype q_dtype, int64_t q_s
                                        window, 0.f, ws + p.decode, dec, fmt, error_flag, stream);
   if (s != KVQ_OK) return s;
   JoinArgs j{a.sh.part, a.sh.ml, (const float*)(ws + p.own), (const float*)(ws + p.lse), cu_groups, prefix_lens,
-             num_groups, num_seqs, nq, p.splits, out, out_dtype == KVQ_DTYPE_BF16};
+             a.sh.unordered, num_groups, num_seqs, nq, p.splits, out, out_dtype == KVQ_DTYPE_BF16};
   const unsigned grid = (unsigned)(((int64_t)num_seqs * nq + 3) / 4);
   if (hd == 64) shared_join_kernel<64><<<grid, 128, 0, st>>>(j);
   else if (hd == 128) shared_join_kernel<128><<<grid, 128, 0, st>>>(j);

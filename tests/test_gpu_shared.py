@@ -236,3 +236,27 @@ def test_shared_pages_freed_before_the_window(hd, bs):
     d["ptab"][0, 60 // bs] = -1
     run(c, d, sliding_window=60, error_flag=err)
     assert err.item() == _abi.KVQ_DEVERR_BLOCK
+
+
+@pytest.mark.parametrize("cu,like", [([0, 4, 2, 6], None), ([2, 1, 6, 6], None), ([0, 6, 5, 4], None),
+                                     ([-3, 2, 4, 6], [0, 2, 4, 6]), ([0, 2, 4, 99], [0, 2, 4, 6])])
+def test_shared_bad_groups_are_flagged(cu, like):
+    """Offsets outside the batch are cut; a decreasing one leaves the prefixes
+    out: the result is that of the sequences' own positions."""
+    c = shared_case("fp8", [300, 64, 200], [2, 2, 2], [5, 0, 33, 1, 70, 9], 8, 2, 128, seed=20)
+    d = dev(c)
+    d["cu"].copy_(torch.tensor(cu, dtype=torch.int32))
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = torch.full((ops.shared_workspace_bytes(6, 3, 8, 2, 128, 16, d["ptab"].shape[1], d["stab"].shape[1], 0, "fp8"),),
+                    0x7E, dtype=torch.uint8, device=DEV)
+    got = run(c, d, workspace=ws, error_flag=err)
+    assert err.item() == _abi.KVQ_DEVERR_RANGE
+    if like is None:
+        want = ops.paged_decode(d["q"], d["kp"], d["vp"], d["stab"], d["slens"], "fp8", 2, 16, k_scale=c["k_scale"],
+                                v_scale=c["v_scale"])
+    else:
+        d["cu"].copy_(torch.tensor(like, dtype=torch.int32))
+        err.zero_()
+        want = run(c, d, error_flag=err)
+        assert err.item() == 0
+    assert torch.equal(got, want)
