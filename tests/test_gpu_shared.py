@@ -260,3 +260,31 @@ def test_shared_bad_groups_are_flagged(cu, like):
         want = run(c, d, error_flag=err)
         assert err.item() == 0
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4", "fp8k_turbo2v"])
+@pytest.mark.parametrize("factor", [2.0 ** 17, 2.0 ** -20])
+def test_shared_query_magnitudes(fmt, factor):
+    """BF16 queries past the range of fp16, above and below, with a score scale
+    that brings the scores back: the same scores, the same result."""
+    c = shared_case(fmt, [300, 37], [3, 2], [5, 0, 33, 1, 70], 8, 2, 128, seed=21)
+    q = torch.from_numpy(c["q"]).to(torch.bfloat16)
+    scale = 128 ** -0.5
+    want = oracle.paged_decode_shared(host(q), c["kc"], c["vc"], c["ptab"], c["plens"], c["cu"], c["stab"], c["slens"],
+                                      2, 128, 16, c["kst"], c["vst"], fmt, k_scale=c["k_scale"], v_scale=c["v_scale"],
+                                      sm_scale=scale)
+    got = run(c, dev(c), q=(q.float() * factor).to(torch.bfloat16).to(DEV), sm_scale=scale / factor)
+    assert_decode_close(host(got), want)
+
+
+@pytest.mark.parametrize("fmt", ALL_FORMATS)
+@pytest.mark.parametrize("hd,nq,nkv", [(64, 4, 2), (128, 8, 2), (256, 4, 2)])
+def test_shared_bf16_io_formats(fmt, hd, nq, nkv):
+    """BF16 queries and outputs (other operand forms than fp32 ones), several
+    ranges of the prefix: the decode's bound and half a step of the output."""
+    c = shared_case(fmt, [700, 90], [3, 2], [5, 0, 33, 1, 70], nq, nkv, hd, seed=hd + 1)
+    d = dev(c)
+    qb = d["q"].to(torch.bfloat16)
+    want = ref(c, q=host(qb))
+    got = host(run(c, d, q=qb, out_dtype=torch.bfloat16))
+    assert (np.abs(got - want) <= 2e-3 + 2.0 ** -8 * np.abs(want)).all()
