@@ -72,7 +72,7 @@ struct SharedArgs {
   const int32_t* own_lens;   // [num_seqs] positions of each sequence after its prefix
   int32_t splits;            // ranges of a prefix at most (partial slots per row)
   float* part;               // [num_seqs][nq][splits][head_dim] unnormalised outputs
-  float2* ml;                // [num_seqs][nq][splits] running maximum (base 2) and sum
+  float2* ml;                // [num_seqs][nq][splits] exponent (base 2) that the outputs are relative to, and sum
   int32_t* counters;         // the decode's merge counters, zeroed for it
   int64_t num_counters;
   int32_t* unordered;        // set to 1 where cu_q (cu_groups) decreases somewhere, else 0

@@ -396,7 +396,7 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
   // does in the other paths: its 8 bits are exact from 2^-17 to 65504, below
   // that it is off by 2^-25 at most (hi + lo parts likewise).  The rest of the
   // scale, [1, 2) then, is taken after the products.  With a 16-bit output
-  // fp16 weights need no lo part (2^-12 of a weight).
+  // fp16 weights need no lo part (2^-12 of a weight, 2^-32 of the largest).
   [[maybe_unused]] bool q_exact = false, p_lo = true;
   [[maybe_unused]] float s_mul = 1.f;   // of the products
   float q_mul = a.score_scale;          // of the queries
@@ -659,16 +659,21 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
 #pragma unroll
     for (int i = 0; i < NS; ++i)
       mx = SH ? t5::max_nan(mx, mx_s[i * C::ROWS + row]) : fmaxf(mx, mx_s[i * C::ROWS + row]);
+    // fp16 weights of a shared prefix are held 2^7 above their size (at most
+    // 2^15, where a row's maximum has grown by 2^8): those of 2^-21 beside the
+    // maximum stay normal numbers and none above 2^-32 is lost, which a long
+    // prefix beside one large weight would add up (l_sum counts them all).
+    constexpr float UP = SH && !VP::BF ? 7.f : 0.f;
     float alpha = 1.f;
     bool resc = false;
     if (mx != -CUDART_INF_F) {
       if (m_used == -CUDART_INF_F) {
-        m_used = mx;
-      } else if (mx > m_used + 8.f) {
-        alpha = t5::ex2(m_used - mx);
+        m_used = mx - UP;
+      } else if (mx > m_used + (8.f + UP)) {
+        alpha = t5::ex2(m_used - (mx - UP));
         resc = true;
         l_sum *= alpha;
-        m_used = mx;
+        m_used = mx - UP;
       }
     }
     const bool live = m_used != -CUDART_INF_F;   // else every score so far is masked: P = 0

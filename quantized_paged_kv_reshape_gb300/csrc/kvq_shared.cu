@@ -3,7 +3,8 @@
 //
 // Sequence s of group g attends to its group's P_g prefix positions, then to
 // its own L_s.  Softmax over both is joined from parts: with (m_i, l_i, o_i)
-// the maximum, sum and unnormalised output of part i of the prefix, and
+// an exponent near the maximum, and the sum and unnormalised output relative
+// to it, of part i of the prefix, and
 // (lse, o) of the sequence's own positions (base 2),
 //   M = max(m_i, lse),  out = (sum 2^(m_i - M) o_i + 2^(lse - M) o) /
 //                             (sum 2^(m_i - M) l_i + 2^(lse - M)).

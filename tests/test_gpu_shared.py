@@ -288,3 +288,33 @@ def test_shared_bf16_io_formats(fmt, hd, nq, nkv):
     want = ref(c, q=host(qb))
     got = host(run(c, d, q=qb, out_dtype=torch.bfloat16))
     assert (np.abs(got - want) <= 2e-3 + 2.0 ** -8 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("first", [True, False])
+def test_shared_small_weights_add_up(out_dtype, first):
+    """One position with nearly all of the weight and a zero value, 4095 with
+    2^-26 of it each and a value of 256: all of the output comes from the small
+    ones.  K and V are exact in FP8 and the scores exact in fp32.
+
+    A weight is held in fp16, at least 2^7 above its size beside the row's
+    maximum: half a step of a subnormal is 2^-25, hence off by at most 2^-32, or
+    2^-12 of itself where it is normal; 2^-18 covers exp2 and the sums, 2^-8 of
+    the result a BF16 output."""
+    n, groups, nq, nkv, hd, bs = 4096, 8, 8, 8, 64, 16
+    k = torch.zeros(n, nkv, hd, device=DEV)
+    v = torch.full((n, nkv, hd), 256.0, device=DEV)
+    one = 0 if first else n - 1
+    k[one, :, 0], v[one] = 1.0, 0.0
+    kp, vp = (ops.alloc_pool(n // bs + 1, "fp8", side, bs, nkv, hd) for side in (0, 1))
+    ops.cache_write(k, v, kp, vp, torch.arange(n, device=DEV), "fp8", nkv, hd, bs)
+    q = torch.zeros(groups, nq, hd, device=DEV, dtype=torch.bfloat16)
+    q[:, :, 0] = 26.0
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    tab = torch.arange(n // bs, dtype=torch.int32, device=DEV).expand(groups, -1).contiguous()
+    out = ops.paged_decode_shared(q, kp, vp, tab, i(*[n] * groups), i(*range(groups + 1)), i(*[0] * groups)[:, None].contiguous(),
+                                  i(*[0] * groups), "fp8", nkv, bs, out_dtype=out_dtype, sm_scale=float(np.log(2.0)))
+    w = 2.0 ** -26 * (n - 1)
+    want = 256.0 * w / (1 + w)
+    tol = 256.0 * n * 2.0 ** -32 + want * (2.0 ** -12 + 2.0 ** -18 + (2.0 ** -8 if out_dtype == torch.bfloat16 else 0))
+    assert np.abs(host(out) - want).max() <= tol
