@@ -436,8 +436,13 @@ kvq_status kvq_paged_decode_shared(
  * ("spark_runtime/kv_cache.rs" layout), so a row's position in the cache does
  * not enter a later decode's scores. */
 
-/* Device scratch kvq_attention_mass needs (any content on entry); depends on
- * the current device's SM count.  0 on an invalid argument. */
+/* Device scratch for kvq_attention_mass (any content on entry); depends on the
+ * current device's SM count.  0 on an invalid argument.  A workspace of this
+ * size also serves calls with a smaller total_q or max_chunk and the other
+ * arguments the same.  Where max_chunk * (num_q_heads / num_kv_heads) <= 8 it
+ * holds the scores of every position the tables have room for (up to 32 bytes
+ * a position and kv head); a call with less room, at least what
+ * max_chunk = 9 needs, reads the keys twice instead. */
 size_t kvq_attention_mass_workspace_bytes(int64_t total_q, int32_t num_seqs, int32_t max_chunk,
                                           int32_t num_q_heads, int32_t num_kv_heads,
                                           int32_t block_size, int32_t max_blocks_per_seq);

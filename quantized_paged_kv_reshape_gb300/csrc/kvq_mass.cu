@@ -85,22 +85,26 @@ cudaError_t launch_mass_add(const MassArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// How a call is cut.  Few rows: enough ranges for about two waves of two CTAs
-// per SM, at most 32 (a warp joins them lane by lane).  Many rows: one CTA per
-// SM, or two ranges per (sequence, kv head) where those alone are more than
-// half the SMs; the kernel balances the ranges over them.
+// How a call is cut.  Few rows (up to 8, with room for their scores): enough
+// ranges for about two waves of two CTAs per SM, at most 32 (a warp joins them
+// lane by lane).  Many rows: one CTA per SM, or two ranges per (sequence, kv
+// head) where those alone are more than half the SMs; the kernel balances the
+// ranges over them.  Its statistics are no larger for a smaller total_q or
+// max_chunk, so that a workspace of a larger chunk always serves: few rows
+// then take the other kernel where their scores do not fit.
 struct MassPlan {
   bool few;
   int splits1, slots, row_pad;
   size_t stats, total;   // bytes of the statistics, and of the workspace
 };
 
-MassPlan mass_plan(int64_t total_q, int32_t num_seqs, int32_t max_chunk, int nq, int nkv, int bs, int32_t max_blocks) {
+MassPlan mass_plan(int64_t total_q, int32_t num_seqs, int32_t max_chunk, int nq, int nkv, int bs, int32_t max_blocks,
+                   bool scores = true) {
   MassPlan p{};
   const int rep = nq / nkv;
   const int64_t rows = (int64_t)max_chunk * rep, units = (int64_t)num_seqs * nkv, max_pos = (int64_t)max_blocks * bs;
   const int64_t tiles = std::max<int64_t>(1, (max_pos + kMassTile - 1) / kMassTile), sms = std::max(sm_count(), 1);
-  p.few = rows <= 8;
+  p.few = scores && rows <= 8;
   if (p.few) {
     p.row_pad = ((int)rows + 1) / 2 * 2;
     p.splits1 = (int)std::max<int64_t>(1, std::min<int64_t>({(4 * sms + units - 1) / units, tiles, 32}));
@@ -165,7 +169,8 @@ kvq_status kvq_attention_mass(const void* q, kvq_dtype q_dtype, int64_t q_stride
   if (k_bstride % 16 || !aligned16(k_cache)) return fail(KVQ_ERR_ALIGN, "cache and block stride must be 16-byte aligned");
   if (ks == S_FP8 && !(k_scale > 0.f && std::isfinite(k_scale)))
     return fail(KVQ_ERR_ARG, "FP8 side needs a finite scale > 0");
-  const MassPlan p = mass_plan(total_q, num_seqs, max_chunk, nq, nkv, bs, max_blocks);
+  MassPlan p = mass_plan(total_q, num_seqs, max_chunk, nq, nkv, bs, max_blocks);
+  if (p.few && workspace_bytes < p.total) p = mass_plan(total_q, num_seqs, max_chunk, nq, nkv, bs, max_blocks, false);
   const size_t need = p.total;
   if (need > 0 && !workspace) return fail(KVQ_ERR_ARG, "null pointer");
   if (workspace_bytes < need) return fail(KVQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace_bytes, need);

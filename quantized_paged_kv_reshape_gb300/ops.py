@@ -340,7 +340,8 @@ def mass_workspace_bytes(total_q, num_seqs, max_chunk, num_q_heads, num_kv_heads
 
 def alloc_mass_workspace(total_q, num_seqs, max_chunk, num_q_heads, num_kv_heads, block_size,
                          max_blocks_per_seq, device="cuda"):
-    """Workspace of attention_mass (any content; one per call in flight)."""
+    """Workspace of attention_mass (any content; one per call in flight).  It also
+    serves calls with fewer queries and the other arguments the same."""
     with torch.cuda.device(device):
         n = mass_workspace_bytes(total_q, num_seqs, max_chunk, num_q_heads, num_kv_heads,
                                  block_size, max_blocks_per_seq)

@@ -525,3 +525,38 @@ def test_evict_streams_and_graphs():
         reset(x)
         g.replay()
         assert all(torch.equal(a, b) for a, b in zip((kp, vp, mass, kept, new), w))
+
+
+def mass_error_bound(c, q, cu, w, scale=None):
+    """The bound of this file's head for totals that start from zero."""
+    lens, nkv, nq, bs, hd = c["lens"], c["nkv"], c["nq"], c["bs"], c["hd"]
+    side = oracle.kv_pair(c["fmt"])[0]
+    qk, q = 0.0, host(q)
+    for s, n in enumerate(int(x) for x in lens):
+        pos = np.arange(n)
+        k = np.abs(oracle.gather_side(c["kc"], side, c["tables"][s, pos // bs], pos % bs, nkv, hd, bs, c["kst"],
+                                      c["k_scale"], to_original_basis=False))
+        qs = q[cu[s]:cu[s + 1]]
+        qs = np.abs(oracle.wht_f64(qs) if oracle.is_wht_rotated(side) else qs)
+        qk = max([qk] + [(qs[:, j] @ k[:, j * nkv // nq].T).max() for j in range(nq)])
+    u = 2.0 ** -24
+    d = (scale or 1 / math.sqrt(hd)) * math.log2(math.e) * qk * (2.0 ** -20 + (hd + 4) * u)
+    rows = max(np.diff(cu)) * nq // nkv
+    return w * (4 * d + 2.0 ** -18) + u * w * (rows + 2)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "turbo4"])
+def test_mass_workspace_of_a_larger_chunk(fmt):
+    """A workspace sized for chunks of 32 queries serves every smaller chunk of
+    the same batch, single queries among them."""
+    lens, nq, nkv, bs = [300, 2000, 17], 8, 2, 16
+    c = decode_case(fmt, lens, nq, nkv, 128, seed=9)
+    kp, _ = pools(c)
+    size = ops.mass_workspace_bytes(3 * 32, 3, 32, nq, nkv, bs, c["tables"].shape[1])
+    for chunk in (32, 3, 2, 1):
+        cu = np.concatenate([[0], np.cumsum([min(chunk, n) for n in lens])]).astype(np.int32)
+        q = t(np.random.default_rng(chunk).standard_normal((int(cu[-1]), nq, 128)).astype(np.float32))
+        out = ops.attention_mass(q, t(cu), chunk, kp, t(c["tables"]), t(c["lens"]), fmt, nkv, bs,
+                                 workspace=torch.full((size,), 0xA5, dtype=torch.uint8, device=DEV))
+        w = oracle.attention_mass(host(q), cu, c["kc"], c["tables"], c["lens"], nkv, 128, bs, c["kst"], fmt, out.shape[2])
+        assert (np.abs(host(out) - w) <= mass_error_bound(c, q, cu, w)).all()
