@@ -138,7 +138,9 @@ __global__ void __launch_bounds__(544, 1) mass_tc_kernel(const MassArgs a, const
   t5::fence_after();
   const uint32_t tmem = *tslot;
   const bool q_lo = side_rotated(S) || !a.q_bf16;
-  const float scale = fabsf(a.score_scale);
+  // (the sign goes into the queries: scores then scale by a positive factor)
+  const float pow2 = BF ? 1.f : t5::pow2_of(a.score_scale), scale = fabsf(a.score_scale) / pow2;
+  const float q_mul = a.score_scale < 0.f ? -pow2 : pow2;
 
   auto load_q = [&](int blk) {   // score rows blk * QR .. into the q planes, 4 rows of a warp at a time
 #pragma unroll 1
@@ -167,11 +169,10 @@ __global__ void __launch_bounds__(544, 1) mass_tc_kernel(const MassArgs a, const
         const int r = r0 + 16 * u;
         if (r >= QR) break;
         if constexpr (side_rotated(S)) fwht_warp<E>(x[u], lane, a.inv_sqrt_hd);
-        const float sgn = a.score_scale < 0.f ? -1.f : 1.f;   // scores then scale by a positive factor
 #pragma unroll
         for (int i = 0; i < E; i += 2) {
           uint32_t h, l;
-          tc::split2<BF>(x[u][i] * sgn, x[u][i + 1] * sgn, h, l);
+          tc::split2<BF>(x[u][i] * q_mul, x[u][i + 1] * q_mul, h, l);
           const int o = sw<QR>(r, lane * E + i);
           *reinterpret_cast<uint32_t*>(smem + o) = h;
           *reinterpret_cast<uint32_t*>(smem + C::QB + o) = l;

@@ -560,3 +560,21 @@ def test_mass_workspace_of_a_larger_chunk(fmt):
                                  workspace=torch.full((size,), 0xA5, dtype=torch.uint8, device=DEV))
         w = oracle.attention_mass(host(q), cu, c["kc"], c["tables"], c["lens"], nkv, 128, bs, c["kst"], fmt, out.shape[2])
         assert (np.abs(host(out) - w) <= mass_error_bound(c, q, cu, w)).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4", "turbo4", "turbo8"])
+@pytest.mark.parametrize("factor", [2.0 ** 17, 2.0 ** -20])
+@pytest.mark.parametrize("chunk", [1, 20])
+def test_mass_query_magnitudes(fmt, factor, chunk):
+    """Queries past the range of fp16, above and below, with a score scale that
+    brings the scores back: the weights of the same queries at size one."""
+    c = decode_case(fmt, [200, 33], 8, 2, 128, seed=10)
+    kp, _ = pools(c)
+    cu = np.array([0, chunk, 2 * chunk], np.int32)
+    q = t(np.random.default_rng(11).standard_normal((2 * chunk, 8, 128)).astype(np.float32))
+    scale = 128 ** -0.5
+    out = ops.attention_mass(q * factor, t(cu), chunk, kp, t(c["tables"]), t(c["lens"]), fmt, 2, 16,
+                             sm_scale=scale / factor, k_scale=c["k_scale"])
+    w = oracle.attention_mass(host(q), cu, c["kc"], c["tables"], c["lens"], 2, 128, 16, c["kst"], fmt, out.shape[2],
+                              k_scale=c["k_scale"], sm_scale=scale)
+    assert (np.abs(host(out) - w) <= mass_error_bound(c, q, cu, w, scale)).all()
