@@ -234,6 +234,12 @@ void set_fast_div(uint32_t d, uint32_t& m, uint32_t& s1, uint32_t& s2) {
 
 }  // namespace
 
+float kvq::query_factor(int k_side, float score_scale) {
+  const float s = std::fabs(score_scale);
+  if (k_side == S_BF16 || !std::isnormal(s) || (s >= 0x1p-14f && s <= 4.f)) return 1.f;
+  return std::ldexp(1.f, std::min(std::ilogb(s) + 6, 127));
+}
+
 int kvq::rmax_for(int rep) { return rep <= 1 ? 1 : rep <= 2 ? 2 : rep <= 4 ? 4 : rep <= 8 ? 8 : 0; }
 
 namespace kvq {

@@ -19,6 +19,14 @@ int sm_count();                 // of the current device, 0 on error
 bool aligned16(const void* p);
 int rmax_for(int rep);          // GQA ratio rounded up to a power of two, 0 above 8
 
+// What queries that become 16-bit operands before the score scale are
+// multiplied by, a power of two (no bits change; the rest of the scale is taken
+// after the products).  1 beside BF16 keys, and for score scales between 2^-14
+// and 4, so for any of a usual model.  Otherwise queries of ordinary scores may
+// lie outside fp16's range (an FP8 scale or sm_scale far from one): the rest of
+// the scale is then in [2^-6, 2^-5), which leaves such queries around one.
+float query_factor(int k_side, float score_scale);
+
 // kvq_paged_decode that also stores each row's base-2 log-sum-exp of the
 // scaled scores (-inf for a row that attends to nothing) when lse is not null.
 kvq_status decode_with_lse(const void* q, kvq_dtype q_dtype, int64_t q_stride, const void* k_cache,

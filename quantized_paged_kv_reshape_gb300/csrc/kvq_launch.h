@@ -71,6 +71,7 @@ struct SharedArgs {
   int32_t num_groups;
   const int32_t* own_lens;   // [num_seqs] positions of each sequence after its prefix
   int32_t splits;            // ranges of a prefix at most (partial slots per row)
+  float q_mul, s_mul;        // queries that are exact 16-bit operands are taken times q_mul, their scores times s_mul
   float* part;               // [num_seqs][nq][splits][head_dim] unnormalised outputs
   float2* ml;                // [num_seqs][nq][splits] exponent (base 2) that the outputs are relative to, and sum
   int32_t* counters;         // the decode's merge counters, zeroed for it

@@ -197,7 +197,9 @@ kvq_status kvq_attention_mass(const void* q, kvq_dtype q_dtype, int64_t q_stride
   a.k_bstride = k_bstride;
   a.k_dsec = kvq_data_section_bytes(fmt, 0, bs, nkv, hd);
   const double scale = sm_scale == 0.f ? 1.0 / std::sqrt((double)hd) : (double)sm_scale;
-  a.score_scale = (float)(scale * M_LOG2E * (ks == S_FP8 ? (double)k_scale : 1.0));
+  const float score_scale = (float)(scale * M_LOG2E * (ks == S_FP8 ? (double)k_scale : 1.0));
+  a.q_mul = query_factor(ks, score_scale);
+  a.score_scale = score_scale / a.q_mul;
   a.inv_sqrt_hd = (float)(1.0 / std::sqrt((double)hd));
   a.window = window;
   a.splits1 = p.splits1;

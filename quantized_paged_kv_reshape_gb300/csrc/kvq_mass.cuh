@@ -22,9 +22,8 @@
 // in operand order, with no staging; q is laid out to match.  Where one
 // 16-bit value is not exact, q and K carry hi + lo fp16 parts (22 bits): the
 // totals are fp32 and add up over many steps, so the decode's 14-bit levels
-// (whose error its 16-bit outputs hide) are not used here.  fp16 queries are
-// taken times the power of two in the score scale, which changes no bits and
-// keeps them in fp16's range where their scores are of an ordinary size.
+// (whose error its 16-bit outputs hide) are not used here.  fp16 queries
+// are kept in range by a power of two (query_factor).
 #pragma once
 
 #include "kvq_prefill_tc5.cuh"
@@ -46,7 +45,7 @@ struct MassArgs {
   int64_t num_blocks;
   int32_t nq, nkv, rep, bs, lbs;
   int64_t k_bstride, k_dsec;
-  float score_scale, inv_sqrt_hd;
+  float score_scale, q_mul, inv_sqrt_hd;   // scores = score_scale * (q_mul * q).k
   int32_t window;
   int32_t splits1;             // position ranges per (sequence, kv head)
   int32_t slots;               // CTAs per kv head (mass_tc_kernel)
@@ -228,7 +227,6 @@ __global__ void __launch_bounds__(32 * kMassWarps) mass_rows_kernel(const MassAr
 
   mass_fill_levels<S>(lv, cb, tid);
   const bool q_lo = side_rotated(S) || !a.q_bf16;
-  const float q_mul = M::BF ? 1.f : t5::pow2_of(a.score_scale), s_mul = a.score_scale / q_mul;
   {   // a warp per score row, into operand order
     const int r = warp;
     float x[E];
@@ -249,7 +247,7 @@ __global__ void __launch_bounds__(32 * kMassWarps) mass_rows_kernel(const MassAr
       const int qc = S == S_BF16 ? (d % 32) / 8 : d / (HD / 4);
       const int idx = S == S_BF16 ? d / 32 * 8 + d % 8 : d % (HD / 4);
       uint32_t h, l;
-      tc::split2<M::BF>(x[i] * q_mul, x[i + 1] * q_mul, h, l);
+      tc::split2<M::BF>(x[i] * a.q_mul, x[i + 1] * a.q_mul, h, l);
       uint32_t* dst = reinterpret_cast<uint32_t*>(qf + (idx / 4) * 32 + r * 4 + qc);
       dst[(idx % 4) / 2] = h;
       dst[2 + (idx % 4) / 2] = l;
@@ -316,10 +314,10 @@ __global__ void __launch_bounds__(32 * kMassWarps) mass_rows_kernel(const MassAr
         tc::mma<M::BF>(sv, kl[0][2 * j], kl[1][2 * j], kl[0][2 * j + 1], kl[1][2 * j + 1], b.x, b.y);
     }
     const int ta = tile * kMassTile + warp * 16 + g, tb = ta + 8;
-    sv[0] = ok0 && ta <= p0 && ta > w0 ? sv[0] * s_mul : -CUDART_INF_F;
-    sv[1] = ok0 && ta <= p1 && ta > w1 ? sv[1] * s_mul : -CUDART_INF_F;
-    sv[2] = ok1 && tb <= p0 && tb > w0 ? sv[2] * s_mul : -CUDART_INF_F;
-    sv[3] = ok1 && tb <= p1 && tb > w1 ? sv[3] * s_mul : -CUDART_INF_F;
+    sv[0] = ok0 && ta <= p0 && ta > w0 ? sv[0] * a.score_scale : -CUDART_INF_F;
+    sv[1] = ok0 && ta <= p1 && ta > w1 ? sv[1] * a.score_scale : -CUDART_INF_F;
+    sv[2] = ok1 && tb <= p0 && tb > w0 ? sv[2] * a.score_scale : -CUDART_INF_F;
+    sv[3] = ok1 && tb <= p1 && tb > w1 ? sv[3] * a.score_scale : -CUDART_INF_F;
     if (2 * c < a.row_pad) {
       if (ta < len) *reinterpret_cast<float2*>(sc_out + (int64_t)ta * a.row_pad + 2 * c) = make_float2(sv[0], sv[1]);
       if (tb < len) *reinterpret_cast<float2*>(sc_out + (int64_t)tb * a.row_pad + 2 * c) = make_float2(sv[2], sv[3]);

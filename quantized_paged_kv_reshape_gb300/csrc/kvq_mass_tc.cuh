@@ -139,8 +139,7 @@ __global__ void __launch_bounds__(544, 1) mass_tc_kernel(const MassArgs a, const
   const uint32_t tmem = *tslot;
   const bool q_lo = side_rotated(S) || !a.q_bf16;
   // (the sign goes into the queries: scores then scale by a positive factor)
-  const float pow2 = BF ? 1.f : t5::pow2_of(a.score_scale), scale = fabsf(a.score_scale) / pow2;
-  const float q_mul = a.score_scale < 0.f ? -pow2 : pow2;
+  const float scale = fabsf(a.score_scale), q_mul = a.score_scale < 0.f ? -a.q_mul : a.q_mul;
 
   auto load_q = [&](int blk) {   // score rows blk * QR .. into the q planes, 4 rows of a warp at a time
 #pragma unroll 1

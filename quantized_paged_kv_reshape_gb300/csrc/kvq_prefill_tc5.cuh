@@ -105,12 +105,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
-// The power of two at or below |x|: a product with it changes no bits (1
-// where x has none that is a normal number).
-__device__ __forceinline__ float pow2_of(float x) {
-  const uint32_t e = __float_as_uint(x) & 0x7f800000u;
-  return e == 0u || e == 0x7f800000u ? 1.f : __uint_as_float(e);
-}
 // Maximum that keeps a NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float y;
@@ -390,23 +384,18 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
   }
 
   // Shared prefixes, where products bound a step more than here: a BF16 q
-  // that is not rotated needs no lo part.  Beside BF16 keys it is the operand
-  // itself; beside fp16 ones (FP8, NVFP4) it is taken times the power of two in
-  // the score scale, which brings it into fp16's range as the whole scale
-  // does in the other paths: its 8 bits are exact from 2^-17 to 65504, below
-  // that it is off by 2^-25 at most (hi + lo parts likewise).  The rest of the
-  // scale, [1, 2) then, is taken after the products.  With a 16-bit output
+  // that is not rotated needs no lo part.  It is the operand as it is, or,
+  // where that is fp16 (FP8, NVFP4 keys) and the score scale far from one,
+  // times a power of two (query_factor); the score scale's rest is taken after
+  // the products.  In fp16 its 8 bits are exact from 2^-17 to 65504, below that
+  // it is off by 2^-25 at most, as hi + lo parts are.  With a 16-bit output
   // fp16 weights need no lo part (2^-12 of a weight, 2^-32 of the largest).
   [[maybe_unused]] bool q_exact = false, p_lo = true;
-  [[maybe_unused]] float s_mul = 1.f;   // of the products
-  float q_mul = a.score_scale;          // of the queries
+  float q_mul = a.score_scale;
   if constexpr (SH) {
     q_exact = !side_rotated(KS) && a.q_bf16;
     p_lo = VP::BF || !a.out_bf16;
-    if (q_exact) {
-      q_mul = KP::BF ? 1.f : t5::pow2_of(a.score_scale);
-      s_mul = a.score_scale / q_mul;
-    }
+    if (q_exact) q_mul = a.sh.q_mul;
   }
   // ---- queries of the tile (rotated when K is), hi/lo planes in K's type
   for (int r = warp; r < C::ROWS; r += NT / 32) {
@@ -420,7 +409,7 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
                         : reinterpret_cast<const float*>(a.q)[off + i];
       if constexpr (side_rotated(KS)) fwht_warp<E>(x, lane, a.inv_sqrt_hd);
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[i] *= q_mul;   // scores come out scaled
+      for (int i = 0; i < E; ++i) x[i] *= q_mul;   // scores come out scaled (or are below)
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i) x[i] = 0.f;
@@ -628,7 +617,7 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
       if constexpr (SH) {
         if (q_exact) {
 #pragma unroll
-          for (int j = 0; j < SC; ++j) sv[j] *= s_mul;
+          for (int j = 0; j < SC; ++j) sv[j] *= a.sh.s_mul;
         }
       }
     }

@@ -221,6 +221,8 @@ kvq_status kvq_paged_decode_shared(const void* q, kvq_dtype q_dtype, int64_t q_s
   a.sh.num_groups = num_groups;
   a.sh.own_lens = seq_lens;
   a.sh.splits = p.splits;
+  a.sh.q_mul = query_factor(ks, a.score_scale);
+  a.sh.s_mul = a.score_scale / a.sh.q_mul;
   a.sh.part = (float*)(ws + p.part);
   a.sh.ml = (float2*)(ws + p.ml);
   // the decode wants its merge counters zero, whatever the workspace held
