@@ -311,6 +311,8 @@ kvq_status kvq::decode_with_lse(const void* q, kvq_dtype q_dtype, int64_t q_stri
   a.k_dsec = kvq_data_section_bytes(fmt, 0, bs, nkv, hd);
   a.v_dsec = kvq_data_section_bytes(fmt, 1, bs, nkv, hd);
   a.score_scale = (float)(scale * M_LOG2E * (ks == S_FP8 ? (double)k_scale : 1.0));
+  a.q_mul = query_factor(ks, a.score_scale);
+  a.score_scale /= a.q_mul;
   a.v_mult = vs == S_FP8 ? v_scale : 1.0f;
   a.inv_sqrt_hd = (float)(1.0 / std::sqrt((double)hd));
   a.window = window;

@@ -898,8 +898,8 @@ decode_tc_kernel(const DecodeArgs a, const Codebooks cb) {
             const int64_t qoff = (int64_t)sq * a.q_stride + (int64_t)(kvh * a.rep + j) * HD + lane * E;
 #pragma unroll
             for (int i = 0; i < E; ++i)
-              xq[i] = a.q_bf16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(a.q)[qoff + i])
-                               : reinterpret_cast<const float*>(a.q)[qoff + i];
+              xq[i] = a.q_mul * (a.q_bf16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(a.q)[qoff + i])
+                                          : reinterpret_cast<const float*>(a.q)[qoff + i]);
             if constexpr (side_rotated(KS)) fwht_warp<E>(xq, lane, a.inv_sqrt_hd);
           } else {
 #pragma unroll

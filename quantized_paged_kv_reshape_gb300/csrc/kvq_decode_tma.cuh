@@ -998,8 +998,8 @@ decode_tma_kernel(const DecodeArgs a, const __grid_constant__ TmaMaps maps, cons
       const int64_t qoff = (int64_t)s_sq * a.q_stride + (int64_t)(kvh * a.rep + j) * HD + lane * E;
 #pragma unroll
       for (int i = 0; i < E; ++i)
-        xq[i] = a.q_bf16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(a.q)[qoff + i])
-                         : reinterpret_cast<const float*>(a.q)[qoff + i];
+        xq[i] = a.q_mul * (a.q_bf16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(a.q)[qoff + i])
+                                    : reinterpret_cast<const float*>(a.q)[qoff + i]);
     }
   };
   // Unit bounds from the CTA loop state (st[0] = next slab of the range,

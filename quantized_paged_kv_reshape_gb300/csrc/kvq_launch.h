@@ -48,7 +48,8 @@ struct DecodeArgs {  // arguments of the paged decode (decode_tc_kernel)
   int32_t nq, nkv, rep;   // rep = nq / nkv
   int32_t bs;
   int64_t k_bstride, v_bstride, k_dsec, v_dsec;
-  float score_scale;      // sm_scale * log2(e) (* k_scale for FP8 K)
+  float q_mul;            // power of two the queries are multiplied by (query_factor)
+  float score_scale;      // sm_scale * log2(e) (* k_scale for FP8 K) / q_mul
   float v_mult;           // v_scale for FP8 V, else 1
   float inv_sqrt_hd;
   int32_t window;

@@ -230,3 +230,17 @@ def test_decode_path_on_gb300():
     assert ops.decode_kernel("bf16k_turbo3v", 128, 8, 16) == ("decode_tma_kernel" if tma else "decode_tc_kernel")
     assert ops.decode_kernel("turbo8", 128, 8, 16) == "decode_tc_kernel"
     assert ops.decode_kernel("turbo4", 256, 8, 16) == "decode_tc_kernel"
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4", "turbo4", "turbo3", "turbo8"])
+@pytest.mark.parametrize("factor", [2.0 ** 17, 2.0 ** -20])
+def test_decode_query_magnitudes(fmt, factor):
+    """Queries past the range of fp16, above and below, with a score scale that
+    brings the scores back: the result of the same queries at size one."""
+    c = decode_case(fmt, [5, 300, 33, 1], 8, 2, 128, seed=22)
+    t = lambda x: torch.from_numpy(x).to("cuda")
+    scale = 128 ** -0.5
+    got = ops.paged_decode(t(c["q"]) * factor, t(c["kc"].reshape(c["num_blocks"], c["kst"])),
+                           t(c["vc"].reshape(c["num_blocks"], c["vst"])), t(c["tables"]), t(c["lens"]), fmt, 2, 16,
+                           sm_scale=scale / factor, k_scale=c["k_scale"], v_scale=c["v_scale"])
+    assert_decode_close(got.double().cpu().numpy(), oracle_decode(c))
