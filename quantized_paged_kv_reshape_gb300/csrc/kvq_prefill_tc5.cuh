@@ -712,9 +712,11 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = 0u;
           }
-          for (int t = 0; t < TOK; ++t) {
+#pragma unroll 1
+          for (int t = 0; t < TOK; ++t) {   // (no branch of a lane's own: tensor-memory accesses are the whole warp's)
             const int pos = st * TOK + t;
-            if (!(row_ok && pos <= p_r && pos >= lo_r && vrow_s[b * TOK + t])) continue;
+            const bool in = row_ok && pos <= p_r && pos >= lo_r && vrow_s[b * TOK + t];
+            if (!__any_sync(0xffffffffu, in)) continue;   // (warp-uniform)
             const int o_ = t5::sw<C::ROWS>(row, t);
             const float p = tc::unpack2<VP::BF>(ph_s[o_]).x + tc::unpack2<VP::BF>(pl_s[o_]).x;
 #pragma unroll
@@ -722,10 +724,10 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
               const int ov = t5::sw<TOK>(t, c0 + j);
               float y = tc::unpack2<VP::BF>(v_s[ov]).x;
               if constexpr (C::VPL == 2) y += tc::unpack2<VP::BF>(v_s[C::VB / 2 + ov]).x;
-              v[j] = __float_as_uint(fmaf(p, y, __uint_as_float(v[j])));
+              const float z = fmaf(p, y, __uint_as_float(v[j]));
+              v[j] = in ? __float_as_uint(z) : v[j];
             }
           }
-          __syncwarp();   // lanes left out other positions; the store is the whole warp's
           t5::st16(o_tm + t_lane + c0, v);
         }
         t5::wait_st();
