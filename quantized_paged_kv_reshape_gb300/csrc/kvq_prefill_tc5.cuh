@@ -388,13 +388,11 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
   // where that is fp16 (FP8, NVFP4 keys) and the score scale far from one,
   // times a power of two (query_factor); the score scale's rest is taken after
   // the products.  In fp16 its 8 bits are exact from 2^-17 to 65504, below that
-  // it is off by 2^-25 at most, as hi + lo parts are.  With a 16-bit output
-  // fp16 weights need no lo part (2^-12 of a weight, 2^-32 of the largest).
-  [[maybe_unused]] bool q_exact = false, p_lo = true;
+  // it is off by 2^-25 at most, as hi + lo parts are.
+  [[maybe_unused]] bool q_exact = false;
   float q_mul = a.score_scale;
   if constexpr (SH) {
     q_exact = !side_rotated(KS) && a.q_bf16;
-    p_lo = VP::BF || !a.out_bf16;
     if (q_exact) q_mul = a.sh.q_mul;
   }
   // ---- queries of the tile (rotated when K is), hi/lo planes in K's type
@@ -652,6 +650,8 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
     // 2^15, where a row's maximum has grown by 2^8): those of 2^-21 beside the
     // maximum stay normal numbers and none above 2^-32 is lost, which a long
     // prefix beside one large weight would add up (l_sum counts them all).
+    // (hi + lo parts for 16-bit outputs too: the hi part alone is off by 2^-11
+    // of a weight, which turns the rounding of some outputs, for 3% of the time.)
     constexpr float UP = SH && !VP::BF ? 7.f : 0.f;
     float alpha = 1.f;
     bool resc = false;
@@ -751,7 +751,7 @@ prefill_tc5_kernel(const PrefillArgs a, const Codebooks cb) {
         for (int j = 0; j < TOK / 16; ++j) {
           const uint32_t op = t5::kstep<C::ROWS>(j), ov = (uint32_t)(j * 2048 / 16);
           tc5::mma_ss<HI>(o_tm, pa + op, va + ov, ID, (st > st_begin || j > 0) ? 1u : 0u);
-          if (!SH || p_lo) tc5::mma_ss<HI>(o_tm, pb + op, va + ov, ID, 1);
+          tc5::mma_ss<HI>(o_tm, pb + op, va + ov, ID, 1);
           if constexpr (C::VPL == 2) tc5::mma_ss<HI>(o_tm, pa + op, vb + ov, ID, 1);
         }
       }

@@ -216,7 +216,6 @@ kvq_status kvq_paged_decode_shared(const void* q, kvq_dtype q_dtype, int64_t q_s
   a.v_mult = vs == S_FP8 ? v_scale : 1.0f;
   a.inv_sqrt_hd = (float)(1.0 / std::sqrt((double)hd));
   a.window = window;
-  a.out_bf16 = out_dtype == KVQ_DTYPE_BF16;   // (the partials are fp32 all the same)
   a.err = error_flag;
   a.sh.num_groups = num_groups;
   a.sh.own_lens = seq_lens;

@@ -297,10 +297,10 @@ def test_shared_small_weights_add_up(out_dtype, first):
     2^-26 of it each and a value of 256: all of the output comes from the small
     ones.  K and V are exact in FP8 and the scores exact in fp32.
 
-    A weight is held in fp16, at least 2^7 above its size beside the row's
-    maximum: half a step of a subnormal is 2^-25, hence off by at most 2^-32, or
-    2^-12 of itself where it is normal; 2^-18 covers exp2 and the sums, 2^-8 of
-    the result a BF16 output."""
+    A weight is held in fp16 parts, 2^7 above its size beside the row's maximum:
+    half a step of a subnormal is 2^-25, hence off by at most 2^-32, or 2^-12 of
+    itself in two parts of 11 bits; 2^-18 covers exp2 and the sums, 2^-8 of the
+    result a BF16 output."""
     n, groups, nq, nkv, hd, bs = 4096, 8, 8, 8, 64, 16
     k = torch.zeros(n, nkv, hd, device=DEV)
     v = torch.full((n, nkv, hd), 256.0, device=DEV)
@@ -318,3 +318,12 @@ def test_shared_small_weights_add_up(out_dtype, first):
     want = 256.0 * w / (1 + w)
     tol = 256.0 * n * 2.0 ** -32 + want * (2.0 ** -12 + 2.0 ** -18 + (2.0 ** -8 if out_dtype == torch.bfloat16 else 0))
     assert np.abs(host(out) - want).max() <= tol
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "turbo4", "nvfp4", "bf16"])
+def test_shared_bf16_outputs_are_the_fp32_ones_rounded(fmt):
+    """The type of the output changes its own rounding alone."""
+    c = shared_case(fmt, [700, 90], [3, 2], [5, 0, 33, 1, 70], 8, 2, 128, seed=23)
+    d = dev(c)
+    for q in (d["q"], d["q"].to(torch.bfloat16)):
+        assert torch.equal(run(c, d, q=q, out_dtype=torch.bfloat16), run(c, d, q=q).to(torch.bfloat16))
