@@ -53,6 +53,11 @@
  *       TURBO8: E E4M3 bytes, then E/16 BF16 scales (little-endian) at
  *              data_section + 2g
  *     A side's block stride (bytes) may exceed kvq_block_bytes (padding).
+ *   - Beside keys that are not BF16, queries become fp16 parts in the decodes
+ *     and the attention mass: with s = sm_scale * log2(e) (* k_scale for FP8
+ *     keys), |q| (rotated where the keys are) has to stay below 65504 where
+ *     2^-14 <= |s| <= 4, and |q s| below 2^9 otherwise.  kvq_paged_prefill
+ *     takes q s as fp16 parts.
  */
 #ifndef KVQ_H_
 #define KVQ_H_
@@ -374,7 +379,10 @@ kvq_status kvq_paged_decode_noalloc(
  *   head_dim 64, 128 or 256; num_q_heads a multiple of num_kv_heads
  *   sm_scale     0 selects 1/sqrt(head_dim)
  * Values at positions a query does not attend to never enter its row, NaN and
- * infinities among them. */
+ * infinities among them.  With BF16 rows and a BF16 out, each softmax weight is
+ * rounded to BF16 for its product with v (2^-8 of a weight, beside the output's
+ * own rounding; the denominator adds the weights up unrounded); an fp32 out
+ * takes the weights in two parts (2^-16).  fp32 rows stay fp32 throughout. */
 kvq_status kvq_prompt_attention(
     const void* q, const void* k, const void* v, kvq_dtype in_dtype,
     int64_t q_stride, int64_t k_stride, int64_t v_stride,
@@ -434,7 +442,9 @@ kvq_status kvq_paged_decode_shared(
  * runs, kvq_evict_select chooses, kvq_cache_compact moves the kept rows to
  * positions 0, 1, ... in their order.  The cache stores keys as attended
  * ("spark_runtime/kv_cache.rs" layout), so a row's position in the cache does
- * not enter a later decode's scores. */
+ * not enter a later decode's scores.  It does enter a sliding window, which
+ * then counts kept rows: the last sliding_window rows of the compacted cache,
+ * whatever their positions were (evict_select's `recent` keeps the last ones). */
 
 /* Device scratch for kvq_attention_mass (any content on entry); depends on the
  * current device's SM count.  0 on an invalid argument.  A workspace of this
@@ -442,7 +452,7 @@ kvq_status kvq_paged_decode_shared(
  * arguments the same.  Where max_chunk * (num_q_heads / num_kv_heads) <= 8 it
  * holds the scores of every position the tables have room for (up to 32 bytes
  * a position and kv head); a call with less room, at least what
- * max_chunk = 9 needs, reads the keys twice instead. */
+ * max_chunk = 9 needs, reads the keys twice instead (about 6 times slower). */
 size_t kvq_attention_mass_workspace_bytes(int64_t total_q, int32_t num_seqs, int32_t max_chunk,
                                           int32_t num_q_heads, int32_t num_kv_heads,
                                           int32_t block_size, int32_t max_blocks_per_seq);
@@ -463,11 +473,12 @@ size_t kvq_attention_mass_workspace_bytes(int64_t total_q, int32_t num_seqs, int
  *                flagged (KVQ_DEVERR_RANGE)
  *   mass_in      device fp32, row (s, h) at (s*num_kv_heads + h)*mass_in_stride,
  *                at least as many columns as are written; NULL = zeros; may be
- *                mass_out itself with the same stride
+ *                mass_out itself with the same stride, but not overlap it
+ *                otherwise
  *   mass_out     positions at or beyond seq_lens[s] are left as they are;
  *                positions at or beyond mass_out_stride are dropped and flagged
- *   workspace    device, 16-byte aligned, >= kvq_attention_mass_workspace_bytes;
- *                calls that may run at the same time need separate ones
+ *   workspace    device, 16-byte aligned, kvq_attention_mass_workspace_bytes (see
+ *                there for less); calls that may run at the same time need separate ones
  * Two launches. */
 kvq_status kvq_attention_mass(
     const void* q, kvq_dtype q_dtype, int64_t q_stride, const int32_t* cu_q, int64_t total_q,
@@ -513,7 +524,7 @@ kvq_status kvq_evict_select(
  *                sequences must not share the moved pages
  *   mass_in, mass_out  NULL, or the weights to move along: mass_out[s, h, i] =
  *                mass_in[s, h, kept[s, h, i]]; mass_out == mass_in only when
- *                moving within the same pages; entries of kept at or beyond
+ *                moving within the same pages, no other overlap; entries of kept at or beyond
  *                mass_in_stride are skipped and flagged (KVQ_DEVERR_RANGE)
  *   block_size 8, 16 or 32; head_dim 64, 128 or 256
  * Block ids outside the pool are skipped and flagged (KVQ_DEVERR_BLOCK). */

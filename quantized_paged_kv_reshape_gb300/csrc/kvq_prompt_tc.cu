@@ -29,11 +29,14 @@
 //     memory; only if the row's grew by more than 2^8 (P <= 2^8 otherwise) is
 //     O rescaled and the weights computed again.
 // One prompt of 16384 tokens, 32 query / 8 kv heads, GB300: head_dim 128
-// 1.43 ms (1.54 PFLOP/s algorithmic, 80% of a cuBLAS burst), 64 1.20 ms; 16
-// heads of 256 2.05 ms (1.07 PFLOP/s).  Bound by each row tile's chain
-// softmax (about 1600 cycles) -> products (1024) -> hand-over (500).
+// 1.38 to 1.52 ms, cold to back to back (1.45 to 1.59 PFLOP/s algorithmic, 75
+// to 83% of a cuBLAS burst), 64 1.17 to 1.20 ms; 16 heads of 256 2.05 to 2.11
+// ms.  Bound by each row tile's chain softmax (about 1600 cycles) -> products
+// (1024) -> hand-over (500).
 // P is rounded to bf16 (relative 2^-8 a weight, the size of the output's own
-// rounding); for an fp32 output it carries hi + lo parts, two products.
+// rounding: 2.1e-3 rms of the output's size where the output's rounding alone
+// gives 1.6e-3); for an fp32 output it carries hi + lo parts, two products
+// (2.46 ms at head_dim 128, 1.69 at 64, 2.64 at 256).
 //
 // A weight of zero does not keep a NaN or infinite value out of a product,
 // so where a tile is cut the warpgroup looks the V tile over and, if it holds
