@@ -235,7 +235,9 @@ size_t kvq_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
  *   q            device, q_dtype, row (s, j) at element s*q_stride + j*head_dim
  *   out          device, out_dtype, contiguous [num_seqs, num_q_heads, head_dim]
  *   block_tables device int32; seq_lens device int32 [num_seqs]
- *   num_blocks   pool size for the block-id check (0 = do not check)
+ *   num_blocks   pool size for the block-id check (0 = do not check).  With a
+ *                window the pages from the 16 positions around lo on are
+ *                checked: with block_size 8 one before lo may be among them
  *   head_dim 64/128/256; num_q_heads % num_kv_heads == 0 with ratio <= 8;
  *   block_size 8, 16 or 32
  *   sm_scale     logit scale; 0 selects 1/sqrt(head_dim)
